@@ -45,8 +45,8 @@ struct cfr_experts {
   uint16_t* xt = nullptr;     // [terms][tokens][hp] bfloat16 terms of x
   uint16_t* h = nullptr;      // [terms][tokens * top][ip] bfloat16 terms of silu(g) u, sorted as order (of w silu(g) u,
                               // in slot order, in a call with few slots)
-  float* yp = nullptr;        // [tokens * top][hp] w_ts D_e h of each slot: float32, or 16-bit integers with
-  uint8_t* ye = nullptr;      // [tokens * top][hp / 64] scales (bfloat16 tokens)
+  float* yp = nullptr;        // [tokens * top][hp] w_ts D_e h of each slot: float32, or float16 with
+  uint8_t* ye = nullptr;      // [tokens * top][hp / 64] powers of two (bfloat16 tokens)
   int32_t* status = nullptr;  // [1]
 };
 
@@ -55,8 +55,10 @@ namespace {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
 union Frag {  // eight bfloat16 values of one lane: its operand of a matrix instruction
   bf16x8_t v;
@@ -494,20 +496,20 @@ __global__ __launch_bounds__(W * 64, 2) void k_experts_up(cfr_experts p, int64_t
   }
 }
 
-// Values stored as 16-bit integers, 32767 for 2^(e - 126): e is the biased
-// exponent of the largest of the block, kept within 32 .. 252 so that both
-// scales are normal floats.
-__device__ __forceinline__ float to_int16(uint32_t e) { return __uint_as_float((253u - e) << 23); }  // 2^(126 - e)
-__device__ __forceinline__ float from_int16(uint32_t e) {
-  return __uint_as_float((e + 1u) << 23) * (1.0f / 32767.0f);  // 2^(e - 126) / 32767
-}
+// Values stored as float16 over a power of two that puts the block's largest
+// finite one, of biased exponent e, at 2^14 or above: e is kept within 15 ..
+// 254, so that both powers are normal floats.
+__device__ __forceinline__ float to_half(uint32_t e) { return __uint_as_float((268u - e) << 23); }    // 2^(141 - e)
+__device__ __forceinline__ float from_half(uint32_t e) { return __uint_as_float((e - 14u) << 23); }  // 2^(e - 141)
 
 // w D h of a tile's slots and 64 W rows, to each slot's own place, in float32;
-// for bfloat16 tokens, whose h was rounded to 2^-8 already, as 16-bit integers
-// with one scale per 64 values: off by at most 2^-15 of the largest of the 64,
-// at half the bytes through memory, written and read again (0.5 GB instead of
-// 1 GB at 4096 tokens of the Qwen3-235B-A22B layer).  A block of 64 with a
-// value of 2^126 or more, or one that is not finite, is NaN as a whole.
+// for bfloat16 tokens, whose h was rounded to 2^-8 already, as float16 with one
+// power of two per 64 values, at half the bytes through memory, written and read
+// again (0.5 GB instead of 1 GB at 4096 tokens of the Qwen3-235B-A22B layer).
+// That rounds each value to 2^-11 of itself, an eighth of y's own rounding,
+// whatever stands beside it: half a step of the smallest float16 numbers is
+// 2^-39 of the largest finite value of the 64, so down to 2^-28 of that the
+// rounding is relative.  An infinity or a NaN is stored as itself.
 // Measured as above: 25, 36 and 430 us; its rows are short, so a workgroup's
 // start and end weigh more than in k_experts_up.
 template <int N, int CF, int KU, int W>
@@ -565,17 +567,35 @@ __global__ __launch_bounds__(W * 64, 2) void k_experts_down(cfr_experts p, int64
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         top = max(top, max(__float_as_uint(acc[0][f][i]) & 0x7FFFFFFFu, __float_as_uint(acc[1][f][i]) & 0x7FFFFFFFu));
-      // rows 4 q + .. of the other lane's half go out in this lane's eights: one scale for both
+      // rows 4 q + .. of the other lane's half go out in this lane's eights: one power for both
       top = max(top, (uint32_t)xor_lane<32>((int)top));
-      const uint32_t e = __float_as_uint(__uint_as_float(top) * w) >> 23 & 255u;
-      const float sc = w * to_int16(min(max(e, 32u), 252u));
-      int16_t* out = reinterpret_cast<int16_t*>(p.yp) + slot * p.hp + pair * 64 + 8 * q;
+      uint32_t e = __float_as_uint(__uint_as_float(top) * w) >> 23 & 255u;
+      float sc = w;
+      // values that are not finite, or so small that sc would not be (sc < 2^15
+      // / top): w goes in first, and the largest of the finite ones counts.  The
+      // two lanes of a column have one top and one w, so both come here or none.
+      if (e == 255u || top < 15u << 23) {
+        top = 0;
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            acc[a][f][i] *= w;
+            const uint32_t m = __float_as_uint(acc[a][f][i]) & 0x7FFFFFFFu;
+            top = max(top, m < 0x7F800000u ? m : 0u);
+          }
+        e = max(top, (uint32_t)xor_lane<32>((int)top)) >> 23;
+        sc = 1.0f;
+      }
+      e = max(e, 15u);
+      sc *= to_half(e);
+      uint16_t* out = reinterpret_cast<uint16_t*>(p.yp) + slot * p.hp + pair * 64 + 8 * q;
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
         uint32_t d[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          d[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pknorm_i16(sc * acc[a][f][2 * i], sc * acc[a][f][2 * i + 1]));
+          d[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{sc * acc[a][f][2 * i], sc * acc[a][f][2 * i + 1]}, f16x2_t));
         u32x4_t r[2];
         eights(d, r);
         if (mine) {
@@ -583,8 +603,7 @@ __global__ __launch_bounds__(W * 64, 2) void k_experts_down(cfr_experts p, int64
           *reinterpret_cast<u32x4_t*>(out + a * 32 + 16) = r[1];
         }
       }
-      // 253 and above (2^126: infinities and NaN among them) make the block NaN
-      if (mine && q == 0) p.ye[slot * (p.hp / 64) + pair] = (uint8_t)max(e, 32u);
+      if (mine && q == 0) p.ye[slot * (p.hp / 64) + pair] = (uint8_t)e;
     }
   }
 }
@@ -617,7 +636,7 @@ __global__ __launch_bounds__(kThreads) void k_experts_combine(cfr_experts p, con
         if (!live[k]) continue;
         const int64_t slot = t * top + s0 + k;
         if constexpr (DT == CFR_BF16) {
-          q[k][0] = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const int16_t*>(p.yp) + slot * p.hp + c);
+          q[k][0] = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const uint16_t*>(p.yp) + slot * p.hp + c);
           e[k] = p.ye[slot * (p.hp / 64) + (c >> 6)];
         } else {
           const u32x4_t* src = reinterpret_cast<const u32x4_t*>(p.yp + slot * p.hp + c);
@@ -628,11 +647,13 @@ __global__ __launch_bounds__(kThreads) void k_experts_combine(cfr_experts p, con
       for (int k = 0; k < kBatch; ++k) {
         if (!live[k]) continue;
         if constexpr (DT == CFR_BF16) {
-          const float sc = e[k] > 252u ? __uint_as_float(0x7FC00000u) : from_int16(e[k]);
+          const float sc = from_half(e[k]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            v[2 * j] = fmaf((float)(int16_t)(q[k][0][j] & 0xFFFFu), sc, v[2 * j]);
-            v[2 * j + 1] = fmaf((float)((int)q[k][0][j] >> 16), sc, v[2 * j + 1]);
+            const uint32_t two = q[k][0][j];  // (a bit cast of the element itself reads the vector's first)
+            const f16x2_t h = __builtin_bit_cast(f16x2_t, two);
+            v[2 * j] = fmaf((float)h.x, sc, v[2 * j]);
+            v[2 * j + 1] = fmaf((float)h.y, sc, v[2 * j + 1]);
           }
         } else {
 #pragma unroll

@@ -481,9 +481,9 @@ int cfr_build_experts(const cfr_experts_config* cfg, const uint8_t* gate_codes, 
  * in float32; silu(G x) * (V x) is rounded before it meets D: to bfloat16 for
  * CFR_BF16 (to 16 bits below 65 routed slots), to 16 bits for CFR_F16, to 24
  * for CFR_F32.  y is rounded once from the float32 sum over the slots; for
- * CFR_BF16 beyond 64 slots that sum is over 16-bit integers with one scale per
- * 64 columns of a slot (off by at most 2^-15 of the 64's largest; 64 columns
- * of a slot that hold an infinity, a NaN or a value of 2^126 or more come out NaN).
+ * CFR_BF16 beyond 64 slots each value of a slot is rounded to 11 bits before
+ * that sum (to at best 2^-39 of the largest finite one among its 64 columns
+ * 64 i .. 64 i + 63).  An infinity or a NaN stays in its column.
  * Results do not depend on timing.  tokens = 0 returns at once.  Calls on one
  * handle share its workspace: order them on one stream; two graphs captured
  * from one handle must not replay at the same time.  Enqueues on `stream`,

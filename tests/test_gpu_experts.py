@@ -10,7 +10,7 @@ pytestmark = [pytest.mark.gpu, pytest.mark.timeout(300)]
 
 torch = pytest.importorskip("torch")
 
-from calibration_free_channel_amd import Experts, ExpertsConfig, mx4_quantize  # noqa: E402
+from calibration_free_channel_amd import Experts, ExpertsConfig, mx4_dequantize, mx4_quantize  # noqa: E402
 from calibration_free_channel_amd._lib import CfrError  # noqa: E402
 from oracle import experts as oracle  # noqa: E402
 
@@ -324,3 +324,76 @@ def test_output_over_an_input_is_refused():
     with pytest.raises(CfrError):
         layer.ex.forward(x, buf.view(torch.int32)[:16].view(8, 2), w, out=out)
     layer.ex.forward(x, ids, buf[8 * 64 : 8 * 64 + 16].view(8, 2), out=out)
+
+
+def _one_channel_layer(d, E=2, top=2, max_tokens=300):
+    """Experts with one channel in use: G reads x[0] times 64, V reads x[1], and
+    d [E, H] is the channel's column of D.  With x[0] = 1, silu(64) is 64 to
+    float32's last bit, so h = 64 x[1] is exact in bfloat16 and a slot's value
+    is w d h up to float32 rounding."""
+    H = d.shape[1]
+    G, V, D = torch.zeros(E, 4, H), torch.zeros(E, 4, H), torch.zeros(E, H, 4)
+    G[:, 0, 0], V[:, 0, 1], D[:, :, 0] = 64.0, 1.0, torch.from_numpy(d).float()
+    q = [mx4_quantize(m.cuda()) for m in (G, V, D)]
+    assert torch.equal(mx4_dequantize(*q[2], 4).cpu(), D)  # d is made of values the format holds
+    return Experts.build(ExpertsConfig(H, E, 4, top, max_tokens), *q)
+
+
+def _one_channel_tokens(T, H, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.zeros(T, H)
+    x[:, 0], x[:, 1] = 1.0, (1.0 + torch.rand(T, generator=g)) * torch.sign(torch.randn(T, generator=g))
+    return x.to(BF16), g
+
+
+@pytest.mark.parametrize("T", [40, 150, 300])  # tiles of 32, 64 and 128 slots
+@pytest.mark.parametrize("spread", [1, 14, 40])
+@pytest.mark.parametrize("shift", [-118, -60, 0, 70])
+def test_slots_products_of_bfloat16_prompts(T, spread, shift):
+    """What a slot's values keep between the product and the sum over the
+    slots.  Rows of D of sizes 2^0 .. 2^(spread - 1) side by side, and two slots
+    that nearly cancel, so that y's own rounding hides nothing.  Each value is
+    rounded to float16 (2^-11 of it) after scaling that puts the largest of its
+    64 at 2^14 or above, where half a step of the smallest float16 numbers,
+    2^-25, is 2^-39 of that largest.  To that come the float32 roundings of w d h
+    and of the sum, 3 * 2^-24 of the values, and y's rounding, 2^-8 of y."""
+    H = 256
+    rng = np.random.default_rng(spread + T)
+    d = rng.choice([1.0, -1.5], (2, H)) * np.exp2(rng.integers(0, spread, H))
+    ex = _one_channel_layer(d)
+    x, g = _one_channel_tokens(T, H, seed=T)
+    u = 1.0 + torch.rand(T, generator=g)
+    w = torch.stack([u, -u * (1 + 2.0 ** -6 * torch.rand(T, generator=g))], 1) * 2.0 ** shift
+    ids = torch.tensor([[0, 1]]).repeat(T, 1).int()
+    y = ex.forward(x.cuda(), ids.cuda(), w.cuda()).double().cpu().numpy()
+    v = w.double().numpy()[:, :, None] * d[None] * (64 * x.double().numpy()[:, 1])[:, None, None]  # [T, slot, H]
+    ref = v.sum(1)
+    top = np.abs(v).reshape(T, 2, H // 64, 64).max(3).repeat(64, 2)
+    tol = (np.abs(v) * (2.0 ** -11 + 3 * 2.0 ** -24) + 2.0 ** -39 * top).sum(1) + np.abs(ref) * 2.0 ** -8
+    tiny = 2.0 ** -126 * 2.0 ** -7 / 2 + 2 * 2.0 ** -126 * 2.0 ** -23  # denormal steps of y and of the slots' values
+    off = np.abs(y - ref) / (tol * (1 + 2.0 ** -7) + tiny)
+    assert off.max() <= 1, off.max()
+    ex.close()
+
+
+@pytest.mark.parametrize("T", [20, 40, 150, 300])  # 20: the path of few slots, which the others agree with
+def test_infinity_in_one_column_leaves_the_others(T):
+    # a value beyond float32 in one column of one slot: that column is infinite,
+    # and its neighbours keep what they would have without it
+    H = 128
+    rng = np.random.default_rng(T)
+    d = rng.choice([1.0, -1.5], (2, H)) * np.exp2(rng.integers(0, 6, (2, H)))
+    d[0, 5] = 2.0 ** 121
+    ex = _one_channel_layer(d)
+    x, g = _one_channel_tokens(T, H, seed=T)
+    w = 4.0 + torch.rand(T, 2, generator=g)
+    ids = torch.tensor([[0, 1]]).repeat(T, 1).int()
+    y = ex.forward(x.cuda(), ids.cuda(), w.cuda()).double().cpu().numpy()
+    h = 64 * x.double().numpy()[:, 1]
+    v = w.double().numpy()[:, :, None] * d[None] * h[:, None, None]
+    assert (y[:, 5] == np.sign(h) * np.inf).all()
+    keep = [c for c in range(H) if c != 5]
+    ref = v.sum(1)[:, keep]
+    tol = np.abs(v).sum(1)[:, keep] * (2.0 ** -11 + 3 * 2.0 ** -24 + 2.0 ** -39 * 2 ** 6) + np.abs(ref) * 2.0 ** -8
+    assert (np.abs(y[:, keep] - ref) <= tol * (1 + 2.0 ** -7)).all()
+    ex.close()
