@@ -397,3 +397,25 @@ def test_infinity_in_one_column_leaves_the_others(T):
     tol = np.abs(v).sum(1)[:, keep] * (2.0 ** -11 + 3 * 2.0 ** -24 + 2.0 ** -39 * 2 ** 6) + np.abs(ref) * 2.0 ** -8
     assert (np.abs(y[:, keep] - ref) <= tol * (1 + 2.0 ** -7)).all()
     ex.close()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_every_token_of_the_largest_call(dtype):
+    # a million slots: each token as it comes out of calls a thirty-second as
+    # large, which take the same tiles; a token's result does not depend on its
+    # place, so they are equal bit for bit
+    layer = Layer(64, 5, 32, 16, max_tokens=65536)
+    T, part = 65536, 2048
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn(T, 64, generator=g).to(dtype).cuda()
+    ids = torch.randint(-1, 5, (T, 16), generator=g).int()
+    ids[:, 5:] = 2  # most slots are one expert's
+    ids, w = ids.cuda(), torch.rand(T, 16, generator=g).cuda()
+    y = layer.ex.forward(x, ids, w)
+    for at in range(0, T, part):
+        s = slice(at, at + part)
+        assert torch.equal(layer.ex.forward(x[s], ids[s], w[s]), y[s]), at
+    for at in (1000, 50000):
+        s = slice(at, at + 40)
+        layer.check(x[s], ids[s], w[s], y[s])
+    layer.ex.close()
