@@ -193,6 +193,14 @@ PyObject* dequantize(PyObject* const* a) {
   return THPVariable_Wrap(std::move(out));
 }
 
+// Leading sizes (all but the last) without the ones before them.
+at::IntArrayRef lead(const at::Tensor& t) {
+  const at::IntArrayRef s = t.sizes().slice(0, t.dim() ? t.dim() - 1 : 0);
+  size_t i = 0;
+  while (i < s.size() && s[i] == 1) ++i;
+  return s.slice(i);
+}
+
 // Pointer and type code of a [cols] weight, or none.
 struct Weight {
   const void* p = nullptr;
@@ -250,7 +258,9 @@ PyObject* norm_out(PyObject* const* a) {
     if (g->dim() != 2 && !g->is_contiguous()) refuse("gate: expected two dimensions, or a contiguous tensor");
     const bool two = g->dim() == 2;
     const int64_t gc = g->dim() ? g->size(-1) : 1, gr = two ? g->size(0) : gc ? g->numel() / gc : 1;
-    if ((gr != 1 && gr != ry.n) || (gc != 1 && gc != ry.cols)) refuse("gate: its shape does not broadcast to y's");
+    // one row or y's rows: the same leading sizes, not only as many rows
+    if ((!lead(*g).empty() && lead(*g) != lead(y)) || (gc != 1 && gc != ry.cols))
+      refuse("gate: its shape does not broadcast to y's");
     n.gate = g->data_ptr();
     n.gate_row_stride = gr > 1 ? two ? g->stride(0) : gc : 0, n.gate_col_stride = gc > 1 ? two ? g->stride(1) : 1 : 0;
   }

@@ -31,10 +31,11 @@ def block_norm_out(y, x, post_weight=None, post_norm=True, gate=None, gate_act="
 
     y [..., cols] is the block's output, x of the same shape (and any of the
     three types) the residual stream.  gate, of y's type: [cols] (or [1, cols])
-    for a gate per channel, [..., 1] for one per token, y's shape for one per
-    value; gate_act is "none", "sigmoid", "silu" or "tanh".  Returns s in x's
-    type (in `out`, which may be x), and with next_norm the pair (s, u), u in
-    next_dtype (y's by default) or in `next_out`."""
+    for a gate per channel, [..., 1] with y's leading sizes for one per token,
+    y's shape for one per value; gate_act is "none", "sigmoid", "silu" or
+    "tanh".  Returns s in x's type (in `out`, which may be x), and with
+    next_norm the pair (s, u), u in next_dtype (y's by default) or in
+    `next_out`."""
     act = GATE_ACTS.get(gate_act)
     if act is None:
         raise ValueError(f"gate_act must be one of {sorted(GATE_ACTS)}")

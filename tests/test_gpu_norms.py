@@ -215,3 +215,21 @@ def test_gate_shapes(shape, gate):
     if y.dim() < 3:
         with pytest.raises(ValueError):
             block_norm_out(y, x, post_norm=False, gate=torch.randn(2, 7).cuda())
+
+
+@pytest.mark.parametrize("shape,gate,as_shape", [
+    ((2, 3, 40), (3, 2, 40), None), ((2, 3, 40), (6, 1, 40), None), ((2, 3, 40), (3, 2, 1), None), ((2, 3, 40), (1, 6, 1), None),
+    ((2, 3, 40), (6, 1), None), ((2, 3, 40), (6, 40), None), ((2, 3, 40), (1, 3, 40), None), ((2, 3, 40), (2, 1, 40), None),
+    ((2, 3, 40), (3, 1), None), ((2, 2, 40), (2, 40), None), ((6, 40), (2, 3, 40), None), ((6, 40), (2, 3, 1), None),
+    ((2, 3, 40), (1, 1, 40), (1, 1, 40)), ((2, 3, 40), (1, 40), (1, 1, 40)), ((2, 3, 40), (40,), (1, 1, 40)),
+    ((2, 3, 40), (1, 1, 1), (1, 1, 1)), ((2, 3, 40), (1, 2, 3, 1), (2, 3, 1)), ((1, 6, 40), (6, 1), (1, 6, 1)),
+    ((1, 6, 40), (6, 40), (1, 6, 40)), ((6, 40), (1, 6, 40), (6, 40)), ((2, 1, 1, 40), (2, 1, 1, 1), (2, 1, 1, 1))])
+def test_gate_rows_are_the_tokens(shape, gate, as_shape):
+    # a gate has one row, or y's rows: the same leading sizes, ones before them
+    # aside, not only as many.  as_shape: how it broadcasts, None: it is refused
+    y, x, g = torch.ones(shape).cuda(), torch.zeros(shape).cuda(), torch.randn(gate).cuda()
+    if as_shape is None:
+        with pytest.raises(ValueError, match="broadcast"):
+            block_norm_out(y, x, post_norm=False, gate=g)
+    else:
+        assert torch.equal(block_norm_out(y, x, post_norm=False, gate=g), g.view(as_shape).expand(shape))
