@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -35,14 +36,20 @@ int code_of(at::ScalarType t) {
   return t == at::kFloat ? CFR_F32 : t == at::kBFloat16 ? CFR_BF16 : t == at::kHalf ? CFR_F16 : -1;
 }
 
-const at::Tensor* optional(PyObject* o, const char* name) {
+// The operators have no backward pass: a tensor that needs a gradient is
+// refused where one would be recorded, unless the result has none by its type
+// (no_grad_lost).
+const at::Tensor* optional(PyObject* o, const char* name, bool no_grad_lost = false) {
   if (o == Py_None) return nullptr;
   if (!THPVariable_Check(o)) refuse("%s: expected a tensor", name);
-  return &THPVariable_Unpack(o);
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (!no_grad_lost && t.requires_grad() && at::GradMode::is_enabled())
+    refuse("%s: needs a gradient, which this operator does not have: detach it, or call under torch.no_grad()", name);
+  return &t;
 }
 
-const at::Tensor& tensor(PyObject* o, const char* name) {
-  const at::Tensor* t = optional(o, name);
+const at::Tensor& tensor(PyObject* o, const char* name, bool no_grad_lost = false) {
+  const at::Tensor* t = optional(o, name, no_grad_lost);
   if (!t) refuse("%s: expected a tensor", name);
   return *t;
 }
@@ -150,7 +157,7 @@ PyObject* pair(PyObject* a, PyObject* b) {
 
 // (x, out) -> (codes, scales)
 PyObject* quantize(PyObject* const* a) {
-  const at::Tensor& x = tensor(a[0], "x");
+  const at::Tensor& x = tensor(a[0], "x", true);  // codes are whole numbers
   const int dt = dtype_code(x, "x");
   const Rows r(x, "x");
   const int dev = x.get_device();

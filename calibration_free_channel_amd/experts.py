@@ -81,7 +81,8 @@ class Experts:
         float16; rows may be strided): the sum over a token's slots of gate_w
         times the slot's expert's down(silu(gate(x)) * up(x)), in x's type.
         expert_ids int32 [tokens, top] (negative: an empty slot), gate_w
-        float32 [tokens, top]."""
+        float32 [tokens, top].  Inference only: tensors that need a gradient
+        are refused while gradients are recorded."""
         c = self.cfg
         args = (self._h.value if self._h else None, c.hidden, c.top, c.device, x, expert_ids, gate_w, out)
         if stream is not None:

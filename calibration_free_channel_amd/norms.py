@@ -14,7 +14,8 @@ def block_norm_in(x, weight=None, eps=1e-6, offset=0.0, out=None, dtype=None, st
     """u = x / sqrt(mean(x^2) + eps) * (offset + weight) over the last
     dimension of x [..., cols] (float32, bfloat16 or float16), in `dtype`
     (x's by default) or in `out`'s; `out` may be x.  Without a weight the
-    factor is one.  Sums in float32."""
+    factor is one.  Sums in float32.  Inference only: tensors that need a
+    gradient are refused while gradients are recorded."""
     if stream is not None:
         return on_stream(stream, x, ops.norm_in, x, weight, eps, offset, out, dtype)
     return ops.norm_in(x, weight, eps, offset, out, dtype)
@@ -35,7 +36,7 @@ def block_norm_out(y, x, post_weight=None, post_norm=True, gate=None, gate_act="
     y's shape for one per value; gate_act is "none", "sigmoid", "silu" or
     "tanh".  Returns s in x's type (in `out`, which may be x), and with
     next_norm the pair (s, u), u in next_dtype (y's by default) or in
-    `next_out`."""
+    `next_out`.  Inference only, as block_norm_in."""
     act = GATE_ACTS.get(gate_act)
     if act is None:
         raise ValueError(f"gate_act must be one of {sorted(GATE_ACTS)}")

@@ -130,3 +130,25 @@ def test_experts_build_refuses_another_devices_stream():
     from calibration_free_channel_amd import Experts, ExpertsConfig
     with pytest.raises(ValueError, match="stream"):
         Experts.build(ExpertsConfig(64, 4, 32, 2), None, None, None, stream=SimpleNamespace(device=torch.device("cuda", 1)))
+
+
+def test_tensors_that_need_gradients_are_refused():
+    # found before the device is looked at, so that host tensors show it
+    torch = pytest.importorskip("torch")
+    from calibration_free_channel_amd import block_norm_in, block_norm_out, mx4_dequantize, mx4_quantize
+    from calibration_free_channel_amd._ext import ops
+    x, g = torch.zeros(4, 32), torch.zeros(4, 32, requires_grad=True)
+    codes = torch.zeros(4, 16, dtype=torch.uint8)
+    ids = torch.zeros(4, 1, dtype=torch.int32)
+    calls = [lambda: block_norm_in(g), lambda: block_norm_out(g, x), lambda: block_norm_out(x, g),
+             lambda: ops.experts_forward(None, 32, 1, 0, g, ids, x[:, :1], None),
+             lambda: ops.experts_forward(None, 32, 1, 0, x, ids, g[:, :1], None)]
+    for call in calls:
+        with pytest.raises(ValueError, match="no_grad"):
+            call()
+        for mode in (torch.no_grad, torch.inference_mode):
+            with mode(), pytest.raises(ValueError, match="device"):
+                call()
+    for call in (lambda: mx4_quantize(g), lambda: mx4_dequantize(codes, codes, 32), lambda: block_norm_in(x)):
+        with pytest.raises(ValueError, match="device"):
+            call()
