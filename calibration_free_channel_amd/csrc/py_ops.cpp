@@ -148,6 +148,13 @@ at::DimVector lead_and(const at::Tensor& t, int64_t last) {
   return s;
 }
 
+// The result as Python sees it.  It may be a caller's tensor: autograd has to
+// find it changed, as after any in-place operation.
+PyObject* written(at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  return THPVariable_Wrap(std::move(t));
+}
+
 PyObject* pair(PyObject* a, PyObject* b) {
   PyObject* r = a && b ? PyTuple_Pack(2, a, b) : nullptr;
   Py_XDECREF(a);
@@ -173,7 +180,7 @@ PyObject* quantize(PyObject* const* a) {
   }
   check(cfr_mx4_quantize(x.data_ptr(), dt, r.n, r.cols, r.stride, static_cast<uint8_t*>(codes.data_ptr()),
                          static_cast<uint8_t*>(scales.data_ptr()), dev, stream_of(dev)));
-  return pair(THPVariable_Wrap(std::move(codes)), THPVariable_Wrap(std::move(scales)));
+  return pair(written(codes), written(scales));
 }
 
 // (codes, scales, cols, dtype, out) -> y
@@ -197,7 +204,7 @@ PyObject* dequantize(PyObject* const* a) {
   const Rows r(out, "out");
   check(cfr_mx4_dequantize(static_cast<const uint8_t*>(codes.data_ptr()), static_cast<const uint8_t*>(scales.data_ptr()),
                            r.n, r.cols, out.data_ptr(), dt, r.stride, dev, stream_of(dev)));
-  return THPVariable_Wrap(std::move(out));
+  return written(out);
 }
 
 // Leading sizes (all but the last) without the ones before them.
@@ -240,7 +247,7 @@ PyObject* norm_in(PyObject* const* a) {
   const Rows ru(out, "out");
   check(cfr_block_norm_in(x.data_ptr(), xd, rx.stride, w.p, w.dt, (float)number(a[3]), (float)number(a[2]), rx.n, rx.cols,
                           out.data_ptr(), ud, ru.stride, dev, stream_of(dev)));
-  return THPVariable_Wrap(std::move(out));
+  return written(out);
 }
 
 // (y, x, post_weight, post_norm, gate, gate_act, out_scale, resid_scale,
@@ -296,8 +303,8 @@ PyObject* norm_out(PyObject* const* a) {
   n.out_scale = (float)number(a[6]), n.resid_scale = (float)number(a[7]);
   n.eps = (float)number(a[10]), n.offset = (float)number(a[11]);
   check(cfr_block_norm_out(&n, stream_of(dev)));
-  PyObject* s = THPVariable_Wrap(std::move(out));
-  return next ? pair(s, THPVariable_Wrap(std::move(u))) : s;
+  PyObject* s = written(out);
+  return next ? pair(s, written(u)) : s;
 }
 
 // (handle, hidden, top, device, x, expert_ids, gate_w, out) -> y
@@ -327,7 +334,7 @@ PyObject* experts_forward(PyObject* const* a) {
   check(cfr_experts_forward(static_cast<cfr_experts*>(h), x.data_ptr(), dt, rx.stride,
                             static_cast<const int32_t*>(ids.data_ptr()), static_cast<const float*>(w.data_ptr()),
                             (int32_t)rx.n, out.data_ptr(), ro.stride, stream_of(dev)));
-  return THPVariable_Wrap(std::move(out));
+  return written(out);
 }
 
 // A function of N positional arguments; nothing it throws leaves this module.

@@ -58,3 +58,26 @@ def test_weights_that_need_gradients_are_quantized():
     want = mx4_quantize(w.detach())
     assert torch.equal(codes, want[0]) and torch.equal(scales, want[1])
     assert not mx4_dequantize(codes, scales, 32).requires_grad
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_writes_count_as_changes(name):
+    # autograd finds a tensor that it saved changed, as after any in-place operation
+    call, _, writes = _calls()[name]
+    before = [t._version for t in writes]
+    call()
+    assert all(t._version == v + 1 for t, v in zip(writes, before))
+    a = torch.randn(4, 32, device="cuda", requires_grad=True)
+    for out in writes:
+        if out.is_floating_point():
+            loss = (a * out).sum()  # saves out
+            call()
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                loss.backward()
+
+
+def test_outputs_made_in_inference_mode():
+    with torch.inference_mode():
+        out = torch.empty(4, 32, device="cuda")
+    x = torch.randn(4, 32, device="cuda")
+    assert block_norm_in(x, out=out) is out and torch.equal(out, block_norm_in(x))
