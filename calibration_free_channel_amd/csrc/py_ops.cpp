@@ -45,6 +45,7 @@ const at::Tensor* optional(PyObject* o, const char* name, bool no_grad_lost = fa
   const at::Tensor& t = THPVariable_Unpack(o);
   if (!no_grad_lost && t.requires_grad() && at::GradMode::is_enabled())
     refuse("%s: needs a gradient, which this operator does not have: detach it, or call under torch.no_grad()", name);
+  if (t.is_neg()) refuse("%s: its memory holds the negative of its values: call resolve_neg()", name);
   return &t;
 }
 

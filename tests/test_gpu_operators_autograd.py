@@ -81,3 +81,19 @@ def test_outputs_made_in_inference_mode():
         out = torch.empty(4, 32, device="cuda")
     x = torch.randn(4, 32, device="cuda")
     assert block_norm_in(x, out=out) is out and torch.equal(out, block_norm_in(x))
+
+
+def test_negated_views_are_refused():
+    # memory that holds the negative of what the tensor stands for
+    x = torch.randn(4, 32, device="cuda")
+    neg = torch._neg_view(x)
+    assert neg.is_neg()
+    with pytest.raises(ValueError, match="resolve_neg"):
+        block_norm_in(neg)
+    with pytest.raises(ValueError, match="resolve_neg"):
+        block_norm_out(x, neg)
+    with pytest.raises(ValueError, match="resolve_neg"):
+        mx4_quantize(neg)
+    with pytest.raises(ValueError, match="resolve_neg"):
+        block_norm_in(x, out=torch._neg_view(torch.empty_like(x)))
+    assert torch.equal(block_norm_in(neg.resolve_neg()), -block_norm_in(x))

@@ -152,3 +152,15 @@ def test_tensors_that_need_gradients_are_refused():
     for call in (lambda: mx4_quantize(g), lambda: mx4_dequantize(codes, codes, 32), lambda: block_norm_in(x)):
         with pytest.raises(ValueError, match="device"):
             call()
+
+
+def test_negated_views_are_refused():
+    # memory that holds the negative of what the tensor stands for
+    torch = pytest.importorskip("torch")
+    from calibration_free_channel_amd import block_norm_in, block_norm_out, mx4_quantize
+    x = torch.zeros(4, 32)
+    neg = torch._neg_view(x)
+    assert neg.is_neg()
+    for call in (lambda: block_norm_in(neg), lambda: block_norm_out(neg, x), lambda: block_norm_out(x, neg), lambda: mx4_quantize(neg)):
+        with pytest.raises(ValueError, match="resolve_neg"):
+            call()
