@@ -1135,7 +1135,10 @@ int cfr_experts_status(cfr_experts* h, int32_t* flags) {
   if ((e = hipDeviceSynchronize()) != hipSuccess) return hipf(e, "status sync");
   if ((e = hipMemcpy(flags, h->status, sizeof(int32_t), hipMemcpyDeviceToHost)) != hipSuccess)
     return hipf(e, "status read");
-  if ((e = hipMemset(h->status, 0, sizeof(int32_t))) != hipSuccess) return hipf(e, "status clear");
+  // waited for: the next call may be on a stream that the null stream does not hold up
+  if ((e = hipMemsetAsync(h->status, 0, sizeof(int32_t), nullptr)) != hipSuccess ||
+      (e = hipStreamSynchronize(nullptr)) != hipSuccess)
+    return hipf(e, "status clear");
   return CFR_OK;
 }
 

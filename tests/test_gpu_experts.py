@@ -419,3 +419,18 @@ def test_every_token_of_the_largest_call(dtype):
         s = slice(at, at + 40)
         layer.check(x[s], ids[s], w[s], y[s])
     layer.ex.close()
+
+
+def test_status_after_status():
+    # the flag of a call made right after the last status(), on a stream of its own, is not lost
+    layer = Layer(64, 4, 32, 2, max_tokens=40)
+    s = torch.cuda.Stream()
+    for T in (2, 40):
+        x, ids, w = layer.tokens(T, BF16)
+        ids[T - 1, 0] = 4
+        torch.cuda.synchronize()
+        for _ in range(50):
+            layer.ex.forward(x, ids, w, stream=s)
+            assert layer.ex.status() == 1
+    assert layer.ex.status() == 0
+    layer.ex.close()
