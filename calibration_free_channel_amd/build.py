@@ -14,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -63,14 +64,32 @@ def build(verbose: bool = False) -> str:
           f"-L{ROCM}/lib", "-lrocsolver", "-lrocblas", "-pthread",
           f"-Wl,-rpath,{ROCM}/lib"], verbose)
     os.replace(tmp, LIB)
-    build_ops(verbose)
+    lacking = ops_lack()
+    if lacking is None:
+        build_ops(verbose)
+    else:
+        if os.path.exists(OPS):
+            os.remove(OPS)  # it was built for another library
+        print(f"_ops.so is not built ({lacking}): the reader works without it, the operators around the block do not",
+              flush=True)
     return LIB
+
+
+def ops_lack() -> str | None:
+    """What the extension module's build would need and is not installed, or None."""
+    try:
+        from torch.utils.cpp_extension import include_paths
+    except ImportError:
+        return "no torch"
+    if not any(os.path.exists(os.path.join(p, "torch", "csrc", "Dtype.h")) for p in include_paths()):
+        return "torch without its headers"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "no Python.h"
+    return None
 
 
 def build_ops(verbose: bool = False) -> str:
     """The extension module, against the installed torch's headers and the libcfr.so beside it."""
-    import sysconfig
-
     import torch
     from torch.utils.cpp_extension import include_paths
     tmp = OPS + ".tmp"
