@@ -17,6 +17,16 @@ if not os.path.exists(os.path.join(_lib.HERE, "_ops.so")):
 _lib.load()
 from . import _ops as ops  # noqa: E402
 
+
+def _check_torch(built, running):
+    # the module reads tensors as that torch's headers lay them out
+    if built != running:
+        raise RuntimeError(f"_ops.so was built for torch {built}, this is {running}: "
+                           "build it again with `python -m calibration_free_channel_amd.build`")
+
+
+_check_torch(ops.torch, str(torch.__version__))
+
 # torch's own way to the current stream's handle builds no Stream object, 1 us less per call
 ops.init(getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream), _lib.check)
 

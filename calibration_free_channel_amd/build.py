@@ -94,7 +94,7 @@ def build_ops(verbose: bool = False) -> str:
     from torch.utils.cpp_extension import include_paths
     tmp = OPS + ".tmp"
     _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", os.path.join(CSRC, "py_ops.cpp"), "-o", tmp,
-          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f'-DCFR_TORCH="{torch.__version__}"',
           *("-isystem" + p for p in include_paths()), "-I" + sysconfig.get_paths()["include"],
           "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python",
           "-L" + HERE, "-l:libcfr.so", "-Wl,-rpath,$ORIGIN"], verbose)

@@ -370,4 +370,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, methods, nullp
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__ops() { return PyModule_Create(&module); }
+// torch: the version whose headers, and so whose layout of tensors, this was built for.
+PyMODINIT_FUNC PyInit__ops() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch", CFR_TORCH) < 0) Py_CLEAR(m);
+  return m;
+}

@@ -164,3 +164,11 @@ def test_negated_views_are_refused():
     for call in (lambda: block_norm_in(neg), lambda: block_norm_out(neg, x), lambda: block_norm_out(x, neg), lambda: mx4_quantize(neg)):
         with pytest.raises(ValueError, match="resolve_neg"):
             call()
+
+
+def test_module_of_another_torch_is_refused():
+    torch = pytest.importorskip("torch")
+    from calibration_free_channel_amd import _ext
+    assert _ext.ops.torch == str(torch.__version__)
+    with pytest.raises(RuntimeError, match="build it again"):
+        _ext._check_torch("1.0.0", _ext.ops.torch)
