@@ -79,7 +79,7 @@ SIGNATURES = {
     "cfr_experts_free": (None, [_P]),
     "cfr_block_norm_in": (c_int32, [_P, c_int32, c_int64, _P, c_int32, c_float, c_float, c_int64, c_int64, _P,
                                     c_int32, c_int64, c_int32, _P]),
-    "cfr_block_norm_out": (c_int32, [_P, _P]),  # CfrNormOutArgs, by reference or as its bytes
+    "cfr_block_norm_out": (c_int32, [_P, _P]),  # CfrNormOutArgs, by reference
     "cfr_last_error": (c_char_p, []),
 }
 
