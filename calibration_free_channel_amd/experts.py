@@ -43,8 +43,9 @@ def _weights(pair, lead, cols, name, device):
 
 class Experts:
     """One layer's routed experts on MXFP4 weights.  Owns device memory until
-    close().  Calls on one object share its workspace: order them on one
-    stream."""
+    close(): the weights, and a workspace for max_tokens tokens (about 6 hidden
+    + top (6 inter + 4 hidden) bytes each).  Calls on one object share the
+    workspace: order them on one stream."""
 
     def __init__(self, handle: ctypes.c_void_p, cfg: ExpertsConfig):
         self._h = handle
@@ -82,7 +83,12 @@ class Experts:
         times the slot's expert's down(silu(gate(x)) * up(x)), in x's type.
         expert_ids int32 [tokens, top] (negative: an empty slot), gate_w
         float32 [tokens, top].  Inference only: tensors that need a gradient
-        are refused while gradients are recorded."""
+        are refused while gradients are recorded.
+
+        x's type chooses what is kept between the products: silu(gate(x)) *
+        up(x) has 24 bits for float32, 16 for float16, and for bfloat16 8 in
+        calls of more than 64 slots (16 below), where a slot's values also
+        have 11 before they are summed in float32."""
         c = self.cfg
         args = (self._h.value if self._h else None, c.hidden, c.top, c.device, x, expert_ids, gate_w, out)
         if stream is not None:

@@ -456,7 +456,10 @@ typedef struct cfr_experts_config {
  * on `stream`, ordered after what is queued there, and returns when it is
  * done; the inputs may then be freed.  On success *out owns about the
  * weights' size in device memory (columns padded to a multiple of 256, rows
- * to one of 256) and a workspace for max_tokens tokens.  Errors: CFR_EINVAL
+ * to one of 256) and a workspace of its own for max_tokens tokens of any type,
+ * 6 H + top (6 I + 4 H) bytes a token (4096 tokens of 4096 values, 8 slots of
+ * 1536 channels: 0.94 GB), so a program that holds many layers sets max_tokens
+ * to the tokens that it feeds them at a time.  Errors: CFR_EINVAL
  * (config, pointers, or a NaN scale among the weights), CFR_ENOMEM, CFR_EHIP;
  * *out is then NULL.
  */

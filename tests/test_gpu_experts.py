@@ -434,3 +434,33 @@ def test_status_after_status():
             assert layer.ex.status() == 1
     assert layer.ex.status() == 0
     layer.ex.close()
+
+
+@pytest.mark.parametrize("T", [40, 150, 300])
+def test_tokens_of_very_different_size_in_one_tile(T):
+    # routing weights of 0, of 2^-120 and ones that carry one column past float32, and
+    # tokens whose h is zero or tiny, between ordinary ones: each token's values
+    # have powers of two of their own
+    H = 128
+    rng = np.random.default_rng(T)
+    d = rng.choice([1.0, -1.5], (2, H)) * np.exp2(rng.integers(0, 6, (2, H)))
+    d[0, 5] = 2.0 ** 70
+    ex = _one_channel_layer(d)
+    x, g = _one_channel_tokens(T, H, seed=T)
+    scale = torch.tensor([1.0, 2.0 ** 60, 0.0, 2.0 ** -120, 1.0, 2.0 ** 30])[torch.randint(0, 6, (T,), generator=g)]
+    x[:, 1] *= torch.tensor([1.0, 1.0, 0.0, 2.0 ** -100])[torch.randint(0, 4, (T,), generator=g)]
+    w = scale[:, None] * (1.0 + torch.rand(T, 2, generator=g))
+    ids = torch.tensor([[0, 1]]).repeat(T, 1).int()
+    y = ex.forward(x.cuda(), ids.cuda(), w.cuda()).double().cpu().numpy()
+    v = w.double().numpy()[:, :, None] * d[None] * (64 * x.double().numpy()[:, 1])[:, None, None]
+    past = np.abs(v) >= 2.0 ** 128
+    assert past.any() and (past.sum(1)[:, [c for c in range(H) if c != 5]] == 0).all()
+    ref = np.where(past, np.copysign(np.inf, v), v).sum(1)
+    kept = np.where(past, 0.0, v)
+    top = np.abs(kept).reshape(T, 2, H // 64, 64).max(3).repeat(64, 2)
+    with np.errstate(invalid="ignore"):
+        tol = (np.abs(kept) * (2.0 ** -11 + 3 * 2.0 ** -24) + 2.0 ** -39 * top).sum(1) + np.abs(ref) * 2.0 ** -8
+        ok = (y == ref) | (np.abs(y - ref) <= tol * (1 + 2.0 ** -7) + 2.0 ** -126)
+    # a y of float32 below 2^128 may round up to bfloat16's infinity: none here is as near
+    assert ok.all(), np.argwhere(~ok)[:5]
+    ex.close()
