@@ -510,7 +510,7 @@ __device__ __forceinline__ float from_half(uint32_t e) { return __uint_as_float(
 // whatever stands beside it: half a step of the smallest float16 numbers is
 // 2^-39 of the largest finite value of the 64, so down to 2^-28 of that the
 // rounding is relative.  An infinity or a NaN is stored as itself.
-// Measured as above: 25, 36 and 430 us; its rows are short, so a workgroup's
+// Measured as above: 28, 37 and 409 us; its rows are short, so a workgroup's
 // start and end weigh more than in k_experts_up.
 template <int N, int CF, int KU, int W>
 __global__ __launch_bounds__(W * 64, 2) void k_experts_down(cfr_experts p, int64_t slots,
