@@ -1089,6 +1089,8 @@ int cfr_experts_forward(cfr_experts* h, const void* x, int32_t dtype, int64_t x_
   if (tokens > 1 && (x_stride < H || y_stride < H)) return fail(CFR_EINVAL, "row strides must be at least hidden");
   if (reinterpret_cast<uintptr_t>(x) % bytes || reinterpret_cast<uintptr_t>(y) % bytes)
     return fail(CFR_EINVAL, "x and y must be aligned to their type");
+  if (reinterpret_cast<uintptr_t>(expert_ids) % 4 || reinterpret_cast<uintptr_t>(gate_w) % 4)
+    return fail(CFR_EINVAL, "expert_ids and gate_w must be aligned to four bytes");
   const Span to = span(y, dtype, y_stride, tokens, H);
   const int64_t routed = (int64_t)tokens * h->cfg.top;  // int32 ids and fp32 weights, four bytes each
   if (overlap(span(x, dtype, x_stride, tokens, H), to) || overlap(span(expert_ids, CFR_F32, routed, 1, routed), to) ||

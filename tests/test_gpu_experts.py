@@ -464,3 +464,20 @@ def test_tokens_of_very_different_size_in_one_tile(T):
     # a y of float32 below 2^128 may round up to bfloat16's infinity: none here is as near
     assert ok.all(), np.argwhere(~ok)[:5]
     ex.close()
+
+
+@pytest.mark.parametrize("T", [4, 40])
+def test_misaligned_pointers_are_refused(T):
+    from calibration_free_channel_amd._lib import CFR_F32, check, load
+    layer = Layer(64, 4, 32, 2, max_tokens=T)
+    x, ids, w = layer.tokens(T, F32)
+    y = torch.zeros_like(x)
+    good = [x.data_ptr(), ids.data_ptr(), w.data_ptr(), y.data_ptr()]
+    for k, off in ((0, 2), (1, 2), (1, 1), (2, 2), (3, 2)):
+        a = list(good)
+        a[k] += off
+        with pytest.raises(CfrError, match="aligned"):
+            check(load().cfr_experts_forward(layer.ex._h, a[0], CFR_F32, 64, a[1], a[2], T, a[3], 64, None))
+    torch.cuda.synchronize()
+    assert (y == 0).all()
+    layer.ex.close()
